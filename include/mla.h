@@ -257,7 +257,9 @@ int mla_decode_sparse_f32(const void* q, const void* kv_cache, int num_pages,
  * lengths, workspace has at least mla_decode_fp8_workspace_size bytes,
  * 256-byte aligned; calls that may overlap (on two streams, in two graphs)
  * need workspaces of their own.  A row with no visible key gets out = 0 and
- * lse = -inf; a page outside the pool is flagged as MLA_ERR_DEVICE_BOUNDS.
+ * lse = -inf; a page outside the pool is flagged as MLA_ERR_DEVICE_BOUNDS; a
+ * tile_meta of another call is flagged as MLA_ERR_PLAN, nothing behind its end
+ * is read, and out and lse stay as they were.
  * Defined by: as mla_decode, over the 8-bit form of its cache.
  * Errors: as mla_decode. */
 int mla_decode_fp8(const void* q, const void* kv_cache, const float* scales, int scale_tokens,

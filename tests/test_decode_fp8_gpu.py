@@ -424,3 +424,42 @@ def test_decode_fp8_many_splits(torch_cuda, h, lens):
     x = Inputs(50 + h, 1, h, lens, 16)
     out, lse, _ = run(torch_cuda, x, f32=True)
     compare(x, out, lse, bars=True)
+
+
+@pytest.mark.parametrize("other", ["bf16", "heads", "batch", "none"])
+@pytest.mark.parametrize("h, lens", [(16, [300]), (128, [5000, 70]), (5, [40] * 300)])
+def test_decode_fp8_plan_of_another_call_leaves_outputs(torch_cuda, other, h, lens):
+    """A plan made for another call, and so shorter than this one's: what lies
+    behind it (here numbers that pass for split counts) is not used, the call is
+    reported, and out and lse stay as they were."""
+    torch, x = torch_cuda, Inputs(51, 1, h, lens, 1)
+    d, B, lib = to_gpu(torch, x), len(lens), libmla.load()
+    stream = torch.cuda.current_stream().cuda_stream
+    need = lib.mla_decode_fp8_plan_size(B, 1, h, 0)
+    buf = torch.full((need // 4 + 64,), 2, dtype=torch.int32, device="cuda")
+    one = d["lens"][:1].contiguous()
+    if other == "bf16":
+        n = lib.mla_plan_size(B, 1, h, 0)
+        rc = lib.mla_decode_plan(d["lens"].data_ptr(), B, 1, h, buf.data_ptr(), n, stream)
+    elif other == "heads":                                       # more tiles, fewer workers in each
+        n = lib.mla_decode_fp8_plan_size(1, 8, 128, 0)
+        rc = lib.mla_decode_fp8_plan(one.data_ptr(), 1, 8, 128, buf.data_ptr(), n, stream)
+    elif other == "batch":
+        n = lib.mla_decode_fp8_plan_size(B + 1, 1, 128, 0)
+        lens2 = torch.cat([d["lens"], d["lens"][:1]])
+        buf = torch.full((max(n, need) // 4 + 64,), 2, dtype=torch.int32, device="cuda")
+        rc = lib.mla_decode_fp8_plan(lens2.data_ptr(), B + 1, 1, 128, buf.data_ptr(), n, stream)
+    else:
+        rc = libmla.MLA_OK
+    assert rc == libmla.MLA_OK
+    out = torch.full((B, 1, h, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((B, h, 1), 7.0, device="cuda")
+    ws = torch.ones(lib.mla_decode_fp8_workspace_size(B, 1, h, 0) // 4 + 64, device="cuda")
+    libmla.mla_check_device_error()
+    rc = lib.mla_decode_fp8(d["q"].data_ptr(), d["codes"].data_ptr(), d["scales"].data_ptr(), 1,
+                            x.pages, d["bt"].data_ptr(), d["bt"].shape[1], d["lens"].data_ptr(), B,
+                            1, h, buf.data_ptr(), out.data_ptr(), lse.data_ptr(), SCALE,
+                            ws.data_ptr(), ws.numel() * 4, stream)
+    assert rc == libmla.MLA_OK
+    assert libmla.mla_check_device_error() == libmla.MLA_ERR_PLAN
+    assert torch.all(out == 7) and torch.all(lse == 7)
