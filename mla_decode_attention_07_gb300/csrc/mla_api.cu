@@ -244,7 +244,8 @@ constexpr int kCombineQuads = 4;    // dim groups (of 4) per job
 // allows).  Six splits at three CTAs per SM, or four at four: the launch picks
 // the form that runs its jobs in fewer waves.
 template <int BATCH, int MINB>
-__global__ void __launch_bounds__(kCombineWarps * 32, MINB) mla_combine_kernel(const DecodeParams p) {
+__global__ void __launch_bounds__(kCombineWarps * 32, MINB)
+    mla_combine_kernel(const DecodeParams p, const int num_clusters) {
   constexpr int kCombineBatch = BATCH;
   // Launched as a programmatic dependent of the decode kernel, whose blocks
   // let this grid launch only after their own wait on the planner had
@@ -260,24 +261,29 @@ __global__ void __launch_bounds__(kCombineWarps * 32, MINB) mla_combine_kernel(c
   // meanwhile its set-up (barriers, TMEM, cluster sync) overlaps this grid.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int32_t* plan = p.plan;
-  __shared__ int s_hdr[4];
+  __shared__ int s_hdr[2];
   __shared__ int s_item[2];
+  const int tiles = plan_tiles(p.s_q, p.h_q), gt = plan_group_clusters(num_clusters, tiles);
   if (threadIdx.x == 0) {
-    s_hdr[0] = __ldcg(plan + H_TILES);
-    s_hdr[1] = __ldcg(plan + H_GT);
-    s_hdr[2] = __ldcg(plan + H_STOTAL);
-    s_hdr[3] = __ldcg(plan + H_NCLUSTERS);
+    s_hdr[0] = __ldcg(plan + H_STOTAL);
+    // A plan of another call (or of the 8-bit decode) may have more slots than
+    // the workspace, or end before this call's items.
+    s_hdr[1] = (__ldcg(plan + H_MAGIC) == kPlanMagic) & (__ldcg(plan + H_BATCH) == p.batch) &
+               (__ldcg(plan + H_SQ) == p.s_q) & (__ldcg(plan + H_HQ) == p.h_q) &
+               (__ldcg(plan + H_TILES) == tiles) & (__ldcg(plan + H_GT) == gt) &
+               (__ldcg(plan + H_NCLUSTERS) == num_clusters);
+    if (!s_hdr[1]) atomicCAS(p.err, 0, MLA_ERR_PLAN);
   }
   __syncthreads();
-  const int tiles = s_hdr[0], gt = s_hdr[1], stotal = s_hdr[2];
+  const int stotal = s_hdr[0];
   const int32_t* items = plan + plan_off_items(gt) / 4;
-  const int64_t max_slots = workspace_slots(s_hdr[3]);
+  const int64_t max_slots = workspace_slots(num_clusters);
   bool waited = false;
   const int rows = p.s_q * p.h_q;
   constexpr int kQuadBlocks = (kDv / 4) / kCombineQuads;   // 32
   const int r = threadIdx.x & (kTileRows - 1);             // tile row of this thread
   const int qpair = threadIdx.x >> 7;                      // dim groups 2 qpair, 2 qpair + 1
-  const int64_t total = (int64_t)p.batch * tiles * kQuadBlocks;
+  const int64_t total = s_hdr[1] ? (int64_t)p.batch * tiles * kQuadBlocks : 0;
   for (int64_t job = blockIdx.x; job < total; job += gridDim.x) {
     const int qb = (int)(job % kQuadBlocks);
     const int64_t item = job / kQuadBlocks;
@@ -940,7 +946,7 @@ const char* mla_strerror(int code) {
 }  // extern "C"
 
 namespace mla {
-cudaError_t launch_combine(const DecodeParams& p, int /*num_clusters*/, int num_sms,
+cudaError_t launch_combine(const DecodeParams& p, int num_clusters, int num_sms,
                            cudaStream_t stream) {
   const int tiles = plan_tiles(p.s_q, p.h_q);
   const int64_t jobs = (int64_t)p.batch * tiles * ((kDv / 4) / kCombineQuads);
@@ -958,7 +964,7 @@ cudaError_t launch_combine(const DecodeParams& p, int /*num_clusters*/, int num_
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return four ? cudaLaunchKernelEx(&cfg, mla_combine_kernel<4, 4>, p)
-              : cudaLaunchKernelEx(&cfg, mla_combine_kernel<6, 3>, p);
+  return four ? cudaLaunchKernelEx(&cfg, mla_combine_kernel<4, 4>, p, num_clusters)
+              : cudaLaunchKernelEx(&cfg, mla_combine_kernel<6, 3>, p, num_clusters);
 }
 }  // namespace mla

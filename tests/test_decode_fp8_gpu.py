@@ -463,3 +463,27 @@ def test_decode_fp8_plan_of_another_call_leaves_outputs(torch_cuda, other, h, le
     assert rc == libmla.MLA_OK
     assert libmla.mla_check_device_error() == libmla.MLA_ERR_PLAN
     assert torch.all(out == 7) and torch.all(lse == 7)
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("h, lens", [(16, [20000]), (128, [5000, 70]), (64, [3000, 10, 2000])])
+def test_bf16_decode_refuses_the_8bit_plan(torch_cuda, h, lens, f32):
+    """The two plans are not interchangeable: that of the 8-bit decode has more
+    workers and so more slots than the bf16 decode's workspace; the call is
+    reported, and out and lse stay as they were."""
+    torch, B = torch_cuda, len(lens)
+    inp = W.make_inputs(131, B, 1, h, lens)
+    t = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()
+    bf = lambda a: t(a.view(np.int16)).view(torch.bfloat16)
+    sl = t(np.asarray(lens, dtype=np.int32))
+    meta, _ = libmla.alloc_fp8_plan_and_workspace(B, 1, h)
+    _, ws = libmla.alloc_plan_and_workspace(B, 1, h)
+    ws.fill_(1.0)
+    libmla.mla_decode_fp8_plan(sl, 1, h, meta)
+    out = torch.full((B, 1, h, 512), 7.0, dtype=torch.float32 if f32 else torch.bfloat16, device="cuda")
+    lse = torch.full((B, h, 1), 7.0, device="cuda")
+    libmla.mla_check_device_error()
+    (libmla.mla_decode_f32 if f32 else libmla.mla_decode)(
+        bf(inp.q), bf(inp.kv_cache), t(inp.block_table), sl, meta, out, lse, inp.softmax_scale, ws)
+    assert libmla.mla_check_device_error() == libmla.MLA_ERR_PLAN
+    assert torch.all(out == 7) and torch.all(lse == 7)
