@@ -1,6 +1,7 @@
 /* Argument marshalling of the rotating appends and the 8-bit-cache decode for
  * Python: reads the tensors' pointers, shapes and strides, refuses what the
- * library could not see (types, shapes, strided tables), and calls the C ABI.
+ * library could not see (types, shapes, strided tables, short plans, tensors on
+ * the host or another device), and calls the C ABI.
  * Plain CPython C API; the functions' addresses come from libmla.py, which has
  * loaded the library.  An 8-bit append takes 5.3 us of a Grace host, its launch
  * 2.1 among them, against 9.3 with the same checks in Python and the call
@@ -17,8 +18,12 @@ static __typeof__(&mla_rope_append_fp8) f_append_fp8;
 static __typeof__(&mla_decode_fp8) f_decode;
 static __typeof__(&mla_decode_fp8_f32) f_decode_f32;
 static __typeof__(&mla_decode_fp8_plan) f_plan;
+static __typeof__(&mla_decode_fp8_plan_size) f_plan_size;
+static int (*f_device)(int*);          /* cudaGetDevice */
+static PyObject* f_stream;             /* torch's current stream of a device */
 
-static PyObject *s_shape, *s_stride, *s_data_ptr, *s_itemsize, *s_contiguous, *s_nbytes;
+static PyObject *s_shape, *s_stride, *s_data_ptr, *s_itemsize, *s_contiguous, *s_nbytes,
+    *s_get_device, *s_cuda_stream;
 
 /* NULL, with a ValueError unless an exception is on its way already. */
 static PyObject* refuse(const char* why) {
@@ -68,6 +73,37 @@ static void* pointer(PyObject* t) {    /* NULL is refused by the library */
   Py_DECREF(x);
   return p;
 }
+/* The current device's number if each of n tensors (NULL and None pass) lies on
+ * it, else -1: the kernels would fault on host memory or another device's. */
+static int on_device(PyObject* const* t, int n) {
+  int64_t at = -1;
+  for (int i = 0; i < n; ++i) {
+    if (!t[i] || t[i] == Py_None) continue;
+    const int64_t d = number(PyObject_CallMethodNoArgs(t[i], s_get_device));
+    if (d < 0 || (at >= 0 && d != at)) return -1;
+    at = d;
+  }
+  int now = -1;
+  return at >= 0 && f_device(&now) == 0 && now == at ? now : -1;
+}
+/* The handle of a stream (a number or torch's object); for None that of torch's
+ * current one, without the object around it (0.1 against 2.9 us a call). */
+static void* stream_of(PyObject* stream, int device) {
+  if (PyLong_Check(stream)) return PyLong_AsVoidPtr(stream);
+  PyObject* x;
+  if (stream == Py_None) {
+    PyObject* d = PyLong_FromLong(device);
+    if (!d) return NULL;
+    x = PyObject_CallOneArg(f_stream, d);
+    Py_DECREF(d);
+  } else {
+    x = PyObject_GetAttr(stream, s_cuda_stream);
+  }
+  if (!x) return NULL;
+  void* p = PyLong_AsVoidPtr(x);
+  Py_DECREF(x);
+  return p;
+}
 static int dim(int64_t v) { return v >= 0 && v <= INT32_MAX; }
 
 /* A cache of pages [pages, 64, 1, 576] with elements of `bytes`. */
@@ -109,6 +145,8 @@ static const char kTable[] = "block_table must be int32 [B, max_pages], contiguo
 static const char kLengths[] = "cache_seqlens and new_lens must be int32 [B], contiguous";
 static const char kCache16[] = "kv_cache must be bf16 [pages, 64, 1, 576], contiguous";
 static const char kCache8[] = "kv_cache must be 8-bit [pages, 64, 1, 576], contiguous";
+static const char kDevice[] = "every tensor must be on the current CUDA device";
+static const char kPlan[] = "tile_meta must be contiguous, of mla_decode_fp8_plan_size bytes";
 static const char kScales[] = "scales must be fp32 [pages, 64 / scale_tokens], contiguous";
 
 /* append(kv_new, kv_cache, scales or None, block_table, cache_seqlens, cos_sin,
@@ -119,7 +157,6 @@ static PyObject* py_append(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   PyObject *kv = a[0], *cache = a[1], *scales = a[2], *table = a[3], *lens = a[4], *cs = a[5],
            *q = a[6], *qo = a[7], *news = a[8];
   const int interleaved = PyObject_IsTrue(a[9]);
-  void* stream = PyLong_AsVoidPtr(a[10]);
   if (PyErr_Occurred()) return NULL;
   const int fp8 = scales != Py_None;
   int64_t ks[3], kt[3], qs[4], qt[4] = {0, 0, 0, 1}, os[4], ot[4] = {0, 0, 0, 1}, cd[2], pages,
@@ -143,6 +180,10 @@ static PyObject* py_append(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   NEED(lengths_ok(lens, ks[0]) && (news == Py_None || lengths_ok(news, ks[0])), kLengths);
   NEED(shape_of(cs, 2, cd) && cd[1] == 64 && dim(cd[0]) && has_type(cs, 4) && contiguous(cs),
        kCosSin);
+  PyObject* const all[] = {kv, cache, scales, table, lens, cs, q, qo, news};
+  const int device = on_device(all, 9);
+  NEED(device >= 0, kDevice);
+  void* stream = stream_of(a[10], device);
   const void *p_kv = pointer(kv), *p_q = queries ? pointer(q) : NULL;
   void *p_qo = queries ? pointer(qo) : NULL, *p_cache = pointer(cache);
   float* p_sc = fp8 ? (float*)pointer(scales) : NULL;
@@ -172,7 +213,6 @@ static PyObject* py_decode(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   PyObject *q = a[1], *cache = a[2], *scales = a[3], *table = a[4], *lens = a[5], *meta = a[6],
            *out = a[7], *lse = a[8], *ws = a[10];
   const double scale = PyFloat_AsDouble(a[9]);
-  void* stream = PyLong_AsVoidPtr(a[11]);
   if (PyErr_Occurred()) return NULL;
   int64_t qs[4], os[4], ls[3], pages, max_pages;
   int g = 0;
@@ -189,6 +229,14 @@ static PyObject* py_decode(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   NEED(scales_ok(scales, pages, &g), kScales);
   NEED(table_ok(table, qs[0], &max_pages), kTable);
   NEED(lengths_ok(lens, qs[0]), kLengths);
+  PyObject* const all[] = {q, cache, scales, table, lens, meta, out, lse, ws};
+  const int device = on_device(all, 9);
+  NEED(device >= 0, kDevice);
+  NEED(contiguous(meta) && number(PyObject_GetAttr(meta, s_nbytes)) >=
+                               (int64_t)f_plan_size((int)qs[0], (int)qs[1], (int)qs[2], device),
+       kPlan);
+  NEED(contiguous(ws), "workspace must be contiguous");
+  void* stream = stream_of(a[11], device);
   const void *p_q = pointer(q), *p_cache = pointer(cache), *p_meta = pointer(meta);
   const float* p_sc = (const float*)pointer(scales);
   const int32_t *p_table = (const int32_t*)pointer(table), *p_lens = (const int32_t*)pointer(lens);
@@ -213,12 +261,16 @@ static PyObject* py_plan(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   (void)self;
   NEED(n == 5, "plan takes 5 arguments");
   const long s_q = PyLong_AsLong(a[1]), h_q = PyLong_AsLong(a[2]);
-  void* stream = PyLong_AsVoidPtr(a[4]);
   if (PyErr_Occurred()) return NULL;
   int64_t batch;
   NEED(shape_of(a[0], 1, &batch) && dim(batch) && has_type(a[0], 4) && contiguous(a[0]),
        "cache_seqlens must be int32 [B], contiguous");
   NEED(dim(s_q) && dim(h_q), "s_q and h_q out of range");
+  PyObject* const all[] = {a[0], a[3]};
+  const int device = on_device(all, 2);
+  NEED(device >= 0, kDevice);
+  NEED(contiguous(a[3]), kPlan);
+  void* stream = stream_of(a[4], device);
   const int32_t* p_lens = (const int32_t*)pointer(a[0]);
   void* p_meta = pointer(a[3]);
   const int64_t bytes = number(PyObject_GetAttr(a[3], s_nbytes));
@@ -230,18 +282,23 @@ static PyObject* py_plan(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   return PyLong_FromLong(rc);
 }
 
-/* bind(five addresses): append, append_fp8, decode, decode_f32, plan */
+/* bind(seven addresses, current_stream): append, append_fp8, decode, decode_f32,
+ * plan, plan_size, cudaGetDevice */
 static PyObject* py_bind(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   (void)self;
-  NEED(n == 5, "bind takes 5 addresses");
-  void* p[5];
-  for (int i = 0; i < 5; ++i) p[i] = PyLong_AsVoidPtr(a[i]);
+  NEED(n == 8, "bind takes 7 addresses and a function");
+  void* p[7];
+  for (int i = 0; i < 7; ++i) p[i] = PyLong_AsVoidPtr(a[i]);
   if (PyErr_Occurred()) return NULL;
   f_append = (__typeof__(f_append))p[0];
   f_append_fp8 = (__typeof__(f_append_fp8))p[1];
   f_decode = (__typeof__(f_decode))p[2];
   f_decode_f32 = (__typeof__(f_decode_f32))p[3];
   f_plan = (__typeof__(f_plan))p[4];
+  f_plan_size = (__typeof__(f_plan_size))p[5];
+  f_device = (__typeof__(f_device))p[6];
+  Py_INCREF(a[7]);
+  Py_XSETREF(f_stream, a[7]);
   Py_RETURN_NONE;
 }
 
@@ -261,7 +318,8 @@ PyMODINIT_FUNC PyInit__binding(void) {
     const char* name;
   } names[] = {{&s_shape, "shape"},       {&s_stride, "stride"},
                {&s_data_ptr, "data_ptr"}, {&s_itemsize, "itemsize"},
-               {&s_contiguous, "is_contiguous"}, {&s_nbytes, "nbytes"}};
+               {&s_contiguous, "is_contiguous"}, {&s_nbytes, "nbytes"},
+               {&s_get_device, "get_device"}, {&s_cuda_stream, "cuda_stream"}};
   for (size_t i = 0; i < sizeof names / sizeof names[0]; ++i) {
     *names[i].to = PyUnicode_InternFromString(names[i].name);
     if (!*names[i].to) return NULL;

@@ -132,9 +132,12 @@ def _load_binding(lib_path: str, lib: ctypes.CDLL) -> None:
     spec = importlib.util.spec_from_file_location("_binding", path)
     mod = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(mod)
+    import torch
     mod.bind(*(ctypes.cast(fn, ctypes.c_void_p).value
                for fn in (lib.mla_rope_append, lib.mla_rope_append_fp8, lib.mla_decode_fp8,
-                          lib.mla_decode_fp8_f32, lib.mla_decode_fp8_plan)))
+                          lib.mla_decode_fp8_f32, lib.mla_decode_fp8_plan,
+                          lib.mla_decode_fp8_plan_size, lib.cudaGetDevice)),
+             torch._C._cuda_getCurrentRawStream)
     _binding = mod
 
 
@@ -367,7 +370,7 @@ def mla_rope_append(kv_new, kv_cache, block_table, cache_seqlens, cos_sin, q_rop
     try:
         rc = (_binding or _fast()).append(kv_new, kv_cache, None, block_table, cache_seqlens,
                                           cos_sin, q_rope, q_out, new_lens, interleaved,
-                                          _stream(stream))
+                                          stream)
     except ValueError as e:
         _refuse("mla_rope_append", e)
     if rc:
@@ -384,7 +387,7 @@ def mla_rope_append_fp8(kv_new, kv_cache, scales, block_table, cache_seqlens, co
     try:
         rc = (_binding or _fast()).append(kv_new, kv_cache, scales, block_table, cache_seqlens,
                                           cos_sin, q_rope, q_out, new_lens, interleaved,
-                                          _stream(stream))
+                                          stream)
     except ValueError as e:
         _refuse("mla_rope_append_fp8", e)
     if rc:
@@ -431,7 +434,7 @@ def mla_decode_fp8_plan(cache_seqlens, s_q: int, h_q: int, tile_meta, stream=Non
     """Device planner of mla_decode_fp8: cache_seqlens int32 [B] and tile_meta
     (alloc_fp8_plan_and_workspace) on the GPU."""
     try:
-        rc = (_binding or _fast()).plan(cache_seqlens, s_q, h_q, tile_meta, _stream(stream))
+        rc = (_binding or _fast()).plan(cache_seqlens, s_q, h_q, tile_meta, stream)
     except ValueError as e:
         _refuse("mla_decode_fp8_plan", e)
     if rc:
@@ -448,7 +451,7 @@ def mla_decode_fp8(q, kv_cache, scales, block_table, cache_seqlens, tile_meta, o
     try:
         rc = (_binding or _fast()).decode(False, q, kv_cache, scales, block_table, cache_seqlens,
                                           tile_meta, out, lse, softmax_scale, workspace,
-                                          _stream(stream))
+                                          stream)
     except ValueError as e:
         _refuse("mla_decode_fp8", e)
     if rc:
@@ -461,7 +464,7 @@ def mla_decode_fp8_f32(q, kv_cache, scales, block_table, cache_seqlens, tile_met
     try:
         rc = (_binding or _fast()).decode(True, q, kv_cache, scales, block_table, cache_seqlens,
                                           tile_meta, out, lse, softmax_scale, workspace,
-                                          _stream(stream))
+                                          stream)
     except ValueError as e:
         _refuse("mla_decode_fp8_f32", e)
     if rc:

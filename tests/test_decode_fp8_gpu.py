@@ -487,3 +487,31 @@ def test_bf16_decode_refuses_the_8bit_plan(torch_cuda, h, lens, f32):
         bf(inp.q), bf(inp.kv_cache), t(inp.block_table), sl, meta, out, lse, inp.softmax_scale, ws)
     assert libmla.mla_check_device_error() == libmla.MLA_ERR_PLAN
     assert torch.all(out == 7) and torch.all(lse == 7)
+
+
+def test_decode_fp8_refuses_short_plans_and_host_tensors(torch_cuda):
+    """A plan's buffer of another shape, strided buffers, and single tensors on
+    the host are refused before anything is enqueued."""
+    torch, x = torch_cuda, Inputs(52, 1, 16, [100], 4)
+    d = to_gpu(torch, x)
+    out = torch.full((1, 1, 16, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((1, 16, 1), 7.0, device="cuda")
+    meta, ws = libmla.alloc_fp8_plan_and_workspace(1, 1, 16)
+    short = libmla.alloc_fp8_plan_and_workspace(1, 1, 128)[0]     # fewer workers in a group
+    good = dict(q=d["q"], kv_cache=d["codes"], scales=d["scales"], block_table=d["bt"],
+                cache_seqlens=d["lens"], tile_meta=meta, out=out, lse=lse, softmax_scale=SCALE,
+                workspace=ws)
+    bad = [dict(tile_meta=short), dict(tile_meta=meta[::2]), dict(tile_meta=meta[:1].expand(1 << 20)),
+           dict(workspace=ws[:1].expand(1 << 28))]
+    bad += [{k: t.cpu()} for k, t in good.items() if k != "softmax_scale"]
+    for kw in bad:
+        with pytest.raises(libmla.MlaError) as e:
+            libmla.mla_decode_fp8(**{**good, **kw})
+        assert e.value.code == libmla.MLA_ERR_INVALID_ARG
+    for a in ((d["lens"].cpu(), meta), (d["lens"], meta.cpu()), (d["lens"], meta[:1].expand(1 << 20))):
+        with pytest.raises(libmla.MlaError) as e:
+            libmla.mla_decode_fp8_plan(a[0], 1, 16, a[1])
+        assert e.value.code == libmla.MLA_ERR_INVALID_ARG
+    assert libmla.mla_check_device_error() == 0
+    assert torch.all(out == 7) and torch.all(lse == 7)
+    assert not np.isnan(run(torch, x, d=d)[0]).any()

@@ -78,3 +78,57 @@ def test_decode_fp8_binding_refuses_wrong_types_and_tables(lib):
         libmla.mla_decode_fp8_f32(**good)                       # its out is fp32
     with pytest.raises(libmla.MlaError):
         libmla.mla_decode_fp8_plan(good["cache_seqlens"].long(), 1, 5, good["tile_meta"], stream=0)
+
+
+class OnDevice:
+    """A tensor as the compiled marshalling sees it, on a device of choice."""
+
+    def __init__(self, t, device):
+        self.t, self.device_index = t, device
+        self.shape, self.dtype, self.itemsize, self.nbytes = tuple(t.shape), t.dtype, t.itemsize, t.nbytes
+
+    def stride(self):
+        return self.t.stride()
+
+    def is_contiguous(self):
+        return self.t.is_contiguous()
+
+    def data_ptr(self):
+        return self.t.data_ptr()
+
+    def get_device(self):
+        return self.device_index
+
+
+def _decode_args(torch):
+    bf, i32 = torch.bfloat16, torch.int32
+    return dict(q=torch.zeros(2, 1, 5, 576, dtype=bf),
+                kv_cache=torch.zeros(4, 64, 1, 576, dtype=torch.uint8), scales=torch.zeros(4, 4),
+                block_table=torch.zeros(2, 2, dtype=i32), cache_seqlens=torch.zeros(2, dtype=i32),
+                tile_meta=torch.zeros(4, dtype=i32), out=torch.zeros(2, 1, 5, 512, dtype=bf),
+                lse=torch.zeros(2, 5, 1), workspace=torch.zeros(4))
+
+
+def test_decode_fp8_binding_refuses_host_tensors(lib):
+    """Every tensor on the host, or one of them among tensors of a device."""
+    torch = pytest.importorskip("torch")
+    good = _decode_args(torch)
+    for host in [set(good)] + [{k} for k in good]:
+        a = {k: t if k in host else OnDevice(t, 0) for k, t in good.items()}
+        with pytest.raises(libmla.MlaError, match="current CUDA device") as e:
+            libmla.mla_decode_fp8(**a, softmax_scale=0.07, stream=0)
+        assert e.value.code == libmla.MLA_ERR_INVALID_ARG
+    for a in ((good["cache_seqlens"], good["tile_meta"]),
+              (OnDevice(good["cache_seqlens"], 0), good["tile_meta"]),
+              (good["cache_seqlens"], OnDevice(good["tile_meta"], 0))):
+        with pytest.raises(libmla.MlaError, match="current CUDA device"):
+            libmla.mla_decode_fp8_plan(a[0], 1, 5, a[1], stream=0)
+
+
+def test_decode_fp8_binding_refuses_two_devices(lib):
+    torch = pytest.importorskip("torch")
+    good = _decode_args(torch)
+    for other in good:
+        a = {k: OnDevice(t, int(k == other)) for k, t in good.items()}
+        with pytest.raises(libmla.MlaError, match="current CUDA device"):
+            libmla.mla_decode_fp8(**a, softmax_scale=0.07, stream=0)

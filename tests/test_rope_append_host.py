@@ -114,3 +114,29 @@ def test_model_e4m3_matches_torch():
     want = torch.from_numpy(x).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
     got = M.e4m3_codes(x)
     assert np.array_equal(M.E4M3[got], M.E4M3[want])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_binding_refuses_host_tensors(lib, fp8):
+    """Every tensor on the host, or one of them among tensors of a device, or
+    one on another device."""
+    from test_decode_fp8_host import OnDevice
+    torch = pytest.importorskip("torch")
+    bf, i32 = torch.bfloat16, torch.int32
+    good = dict(kv_new=torch.zeros(2, 3, 576, dtype=bf),
+                kv_cache=torch.zeros(4, 64, 1, 576, dtype=torch.uint8 if fp8 else bf),
+                block_table=torch.zeros(2, 2, dtype=i32), cache_seqlens=torch.zeros(2, dtype=i32),
+                cos_sin=torch.zeros(64, 64), q_rope=torch.zeros(2, 3, 5, 64, dtype=bf),
+                q_out=torch.zeros(2, 3, 5, 64, dtype=bf), new_lens=torch.zeros(2, dtype=i32))
+    if fp8:
+        good["scales"] = torch.zeros(4, 4)
+    fn = libmla.mla_rope_append_fp8 if fp8 else libmla.mla_rope_append
+    for odd in [set(good)] + [{k} for k in good]:
+        for other in (None, 1):
+            if other and len(odd) > 1:
+                continue
+            a = {k: OnDevice(t, 0) if k not in odd else OnDevice(t, other) if other else t
+                 for k, t in good.items()}
+            with pytest.raises(libmla.MlaError, match="current CUDA device") as e:
+                fn(**a, stream=0)
+            assert e.value.code == libmla.MLA_ERR_INVALID_ARG
