@@ -22,8 +22,11 @@ static __typeof__(&mla_decode_fp8_plan_size) f_plan_size;
 static int (*f_device)(int*);          /* cudaGetDevice */
 static PyObject* f_stream;             /* torch's current stream of a device */
 
-static PyObject *s_shape, *s_stride, *s_data_ptr, *s_itemsize, *s_contiguous, *s_nbytes,
+static PyObject *s_shape, *s_stride, *s_data_ptr, *s_dtype, *s_contiguous, *s_nbytes,
     *s_get_device, *s_cuda_stream;
+
+/* torch's types, an object each; e4m3 codes may also come as bytes. */
+static PyObject *t_bf16[2], *t_f32[2], *t_i32[2], *t_e4m3[2];
 
 /* NULL, with a ValueError unless an exception is on its way already. */
 static PyObject* refuse(const char* why) {
@@ -57,8 +60,11 @@ static int64_t number(PyObject* x) {   /* -1 on an error */
   Py_DECREF(x);
   return v;
 }
-static int has_type(PyObject* t, int bytes) {
-  return number(PyObject_GetAttr(t, s_itemsize)) == bytes;
+static int has_type(PyObject* t, PyObject* const* type) {
+  PyObject* x = PyObject_GetAttr(t, s_dtype);
+  const int ok = x && (x == type[0] || x == type[1]);
+  Py_XDECREF(x);
+  return ok;
 }
 static int contiguous(PyObject* t) {
   PyObject* x = PyObject_CallMethodNoArgs(t, s_contiguous);
@@ -106,12 +112,12 @@ static void* stream_of(PyObject* stream, int device) {
 }
 static int dim(int64_t v) { return v >= 0 && v <= INT32_MAX; }
 
-/* A cache of pages [pages, 64, 1, 576] with elements of `bytes`. */
-static int cache_ok(PyObject* t, int bytes, int64_t* pages) {
+/* A cache of pages [pages, 64, 1, 576]. */
+static int cache_ok(PyObject* t, PyObject* const* type, int64_t* pages) {
   int64_t s[4];
   *pages = 0;
   if (!shape_of(t, 4, s) || s[1] != 64 || s[2] != 1 || s[3] != 576 || !dim(s[0]) ||
-      !has_type(t, bytes) || !contiguous(t))
+      !has_type(t, type) || !contiguous(t))
     return 0;
   *pages = s[0];
   return 1;
@@ -120,21 +126,21 @@ static int cache_ok(PyObject* t, int bytes, int64_t* pages) {
 static int scales_ok(PyObject* t, int64_t pages, int* scale_tokens) {
   int64_t s[2];
   if (!shape_of(t, 2, s) || s[0] != pages || s[1] < 1 || s[1] > 64 || 64 % s[1] != 0 ||
-      !has_type(t, 4) || !contiguous(t))
+      !has_type(t, t_f32) || !contiguous(t))
     return 0;
   *scale_tokens = (int)(64 / s[1]);
   return 1;
 }
 static int table_ok(PyObject* t, int64_t batch, int64_t* max_pages) {
   int64_t s[2];
-  if (!shape_of(t, 2, s) || s[0] < batch || !dim(s[1]) || !has_type(t, 4) || !contiguous(t))
+  if (!shape_of(t, 2, s) || s[0] < batch || !dim(s[1]) || !has_type(t, t_i32) || !contiguous(t))
     return 0;
   *max_pages = s[1];
   return 1;
 }
 static int lengths_ok(PyObject* t, int64_t batch) {
   int64_t n;
-  return shape_of(t, 1, &n) && n >= batch && has_type(t, 4) && contiguous(t);
+  return shape_of(t, 1, &n) && n >= batch && has_type(t, t_i32) && contiguous(t);
 }
 
 static const char kKvNew[] = "kv_new must be bf16 [B, s_new, 576], its last dim contiguous";
@@ -144,7 +150,7 @@ static const char kCosSin[] = "cos_sin must be fp32 [max_positions, 64], contigu
 static const char kTable[] = "block_table must be int32 [B, max_pages], contiguous";
 static const char kLengths[] = "cache_seqlens and new_lens must be int32 [B], contiguous";
 static const char kCache16[] = "kv_cache must be bf16 [pages, 64, 1, 576], contiguous";
-static const char kCache8[] = "kv_cache must be 8-bit [pages, 64, 1, 576], contiguous";
+static const char kCache8[] = "kv_cache must be float8_e4m3fn or uint8 [pages, 64, 1, 576], contiguous";
 static const char kDevice[] = "every tensor must be on the current CUDA device";
 static const char kPlan[] = "tile_meta must be contiguous, of mla_decode_fp8_plan_size bytes";
 static const char kScales[] = "scales must be fp32 [pages, 64 / scale_tokens], contiguous";
@@ -163,7 +169,7 @@ static PyObject* py_append(PyObject* self, PyObject* const* a, Py_ssize_t n) {
           max_pages;
   int g = 0;
   NEED(shape_of(kv, 3, ks) && ks[2] == 576 && dim(ks[0]) && dim(ks[1]) && strides_of(kv, 3, kt) &&
-           kt[2] == 1 && has_type(kv, 2),
+           kt[2] == 1 && has_type(kv, t_bf16),
        kKvNew);
   const int queries = q != Py_None;
   NEED(queries == (qo != Py_None), kQueries);
@@ -171,14 +177,14 @@ static PyObject* py_append(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     NEED(shape_of(q, 4, qs) && qs[0] == ks[0] && qs[1] == ks[1] && dim(qs[2]) && qs[3] == 64 &&
              shape_of(qo, 4, os) && os[0] == qs[0] && os[1] == qs[1] && os[2] == qs[2] &&
              os[3] == 64 && strides_of(q, 4, qt) && strides_of(qo, 4, ot) && qt[3] == 1 &&
-             ot[3] == 1 && has_type(q, 2) && has_type(qo, 2),
+             ot[3] == 1 && has_type(q, t_bf16) && has_type(qo, t_bf16),
          kQueries);
   }
-  NEED(cache_ok(cache, fp8 ? 1 : 2, &pages), fp8 ? kCache8 : kCache16);
+  NEED(cache_ok(cache, fp8 ? t_e4m3 : t_bf16, &pages), fp8 ? kCache8 : kCache16);
   if (fp8) NEED(scales_ok(scales, pages, &g), kScales);
   NEED(table_ok(table, ks[0], &max_pages), kTable);
   NEED(lengths_ok(lens, ks[0]) && (news == Py_None || lengths_ok(news, ks[0])), kLengths);
-  NEED(shape_of(cs, 2, cd) && cd[1] == 64 && dim(cd[0]) && has_type(cs, 4) && contiguous(cs),
+  NEED(shape_of(cs, 2, cd) && cd[1] == 64 && dim(cd[0]) && has_type(cs, t_f32) && contiguous(cs),
        kCosSin);
   PyObject* const all[] = {kv, cache, scales, table, lens, cs, q, qo, news};
   const int device = on_device(all, 9);
@@ -217,15 +223,15 @@ static PyObject* py_decode(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   int64_t qs[4], os[4], ls[3], pages, max_pages;
   int g = 0;
   NEED(shape_of(q, 4, qs) && dim(qs[0]) && dim(qs[1]) && dim(qs[2]) && qs[3] == 576 &&
-           has_type(q, 2) && contiguous(q),
+           has_type(q, t_bf16) && contiguous(q),
        "q must be bf16 [B, s_q, h_q, 576], contiguous");
   NEED(shape_of(out, 4, os) && os[0] == qs[0] && os[1] == qs[1] && os[2] == qs[2] && os[3] == 512 &&
-           has_type(out, f32 ? 4 : 2) && contiguous(out),
+           has_type(out, f32 ? t_f32 : t_bf16) && contiguous(out),
        "out must be [B, s_q, h_q, 512] of the call's type, contiguous");
   NEED(shape_of(lse, 3, ls) && ls[0] == qs[0] && ls[1] == qs[2] && ls[2] == qs[1] &&
-           has_type(lse, 4) && contiguous(lse),
+           has_type(lse, t_f32) && contiguous(lse),
        "lse must be fp32 [B, h_q, s_q], contiguous");
-  NEED(cache_ok(cache, 1, &pages), kCache8);
+  NEED(cache_ok(cache, t_e4m3, &pages), kCache8);
   NEED(scales_ok(scales, pages, &g), kScales);
   NEED(table_ok(table, qs[0], &max_pages), kTable);
   NEED(lengths_ok(lens, qs[0]), kLengths);
@@ -263,7 +269,7 @@ static PyObject* py_plan(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   const long s_q = PyLong_AsLong(a[1]), h_q = PyLong_AsLong(a[2]);
   if (PyErr_Occurred()) return NULL;
   int64_t batch;
-  NEED(shape_of(a[0], 1, &batch) && dim(batch) && has_type(a[0], 4) && contiguous(a[0]),
+  NEED(shape_of(a[0], 1, &batch) && dim(batch) && has_type(a[0], t_i32) && contiguous(a[0]),
        "cache_seqlens must be int32 [B], contiguous");
   NEED(dim(s_q) && dim(h_q), "s_q and h_q out of range");
   PyObject* const all[] = {a[0], a[3]};
@@ -282,11 +288,12 @@ static PyObject* py_plan(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   return PyLong_FromLong(rc);
 }
 
-/* bind(seven addresses, current_stream): append, append_fp8, decode, decode_f32,
- * plan, plan_size, cudaGetDevice */
+/* bind(seven addresses, current_stream, five types): append, append_fp8, decode,
+ * decode_f32, plan, plan_size, cudaGetDevice; bfloat16, float32, int32,
+ * float8_e4m3fn, uint8 */
 static PyObject* py_bind(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   (void)self;
-  NEED(n == 8, "bind takes 7 addresses and a function");
+  NEED(n == 13, "bind takes 7 addresses, a function and 5 types");
   void* p[7];
   for (int i = 0; i < 7; ++i) p[i] = PyLong_AsVoidPtr(a[i]);
   if (PyErr_Occurred()) return NULL;
@@ -299,6 +306,14 @@ static PyObject* py_bind(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   f_device = (__typeof__(f_device))p[6];
   Py_INCREF(a[7]);
   Py_XSETREF(f_stream, a[7]);
+  PyObject** const to[] = {t_bf16, t_f32, t_i32, t_e4m3};
+  for (int i = 0; i < 4; ++i) {
+    for (int k = 0; k < 2; ++k) {
+      PyObject* type = a[i == 3 && k ? 12 : 8 + i];
+      Py_INCREF(type);
+      Py_XSETREF(to[i][k], type);
+    }
+  }
   Py_RETURN_NONE;
 }
 
@@ -317,7 +332,7 @@ PyMODINIT_FUNC PyInit__binding(void) {
     PyObject** to;
     const char* name;
   } names[] = {{&s_shape, "shape"},       {&s_stride, "stride"},
-               {&s_data_ptr, "data_ptr"}, {&s_itemsize, "itemsize"},
+               {&s_data_ptr, "data_ptr"}, {&s_dtype, "dtype"},
                {&s_contiguous, "is_contiguous"}, {&s_nbytes, "nbytes"},
                {&s_get_device, "get_device"}, {&s_cuda_stream, "cuda_stream"}};
   for (size_t i = 0; i < sizeof names / sizeof names[0]; ++i) {

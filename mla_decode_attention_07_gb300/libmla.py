@@ -137,7 +137,8 @@ def _load_binding(lib_path: str, lib: ctypes.CDLL) -> None:
                for fn in (lib.mla_rope_append, lib.mla_rope_append_fp8, lib.mla_decode_fp8,
                           lib.mla_decode_fp8_f32, lib.mla_decode_fp8_plan,
                           lib.mla_decode_fp8_plan_size, lib.cudaGetDevice)),
-             torch._C._cuda_getCurrentRawStream)
+             torch._C._cuda_getCurrentRawStream, torch.bfloat16, torch.float32, torch.int32,
+             torch.float8_e4m3fn, torch.uint8)
     _binding = mod
 
 

@@ -132,3 +132,32 @@ def test_decode_fp8_binding_refuses_two_devices(lib):
         a = {k: OnDevice(t, int(k == other)) for k, t in good.items()}
         with pytest.raises(libmla.MlaError, match="current CUDA device"):
             libmla.mla_decode_fp8(**a, softmax_scale=0.07, stream=0)
+
+
+def test_decode_fp8_binding_refuses_types_of_the_same_size(lib):
+    """A type is more than its size: each tensor in every other type of as many
+    bytes an element, on the device and else as it should be."""
+    torch = pytest.importorskip("torch")
+    same = {1: [torch.int8, torch.float8_e5m2, torch.float8_e4m3fnuz, torch.bool],
+            2: [torch.float16, torch.int16], 4: [torch.int32, torch.float32]}
+    good = _decode_args(torch)
+    needs = dict(q="q must be bf16", kv_cache="kv_cache must be float8_e4m3fn or uint8",
+                 scales="scales must be fp32", block_table="block_table must be int32",
+                 cache_seqlens="must be int32", out="out must be", lse="lse must be fp32")
+    for k, why in needs.items():
+        for other in same[good[k].itemsize]:
+            if other == good[k].dtype:
+                continue
+            a = {**{n: OnDevice(t, 0) for n, t in good.items()}, k: OnDevice(good[k].view(other), 0)}
+            with pytest.raises(libmla.MlaError, match=why) as e:
+                libmla.mla_decode_fp8(**a, softmax_scale=0.07, stream=0)
+            assert e.value.code == libmla.MLA_ERR_INVALID_ARG
+    with pytest.raises(libmla.MlaError, match="out must be"):        # its own type is fp32
+        libmla.mla_decode_fp8_f32(**good, softmax_scale=0.07, stream=0)
+    with pytest.raises(libmla.MlaError, match="must be int32"):
+        libmla.mla_decode_fp8_plan(OnDevice(torch.zeros(2), 0), 1, 5, OnDevice(good["tile_meta"], 0),
+                                   stream=0)
+    # both types of codes reach the check of devices
+    for codes in (good["kv_cache"], good["kv_cache"].view(torch.float8_e4m3fn)):
+        with pytest.raises(libmla.MlaError, match="current CUDA device"):
+            libmla.mla_decode_fp8(**{**good, "kv_cache": codes}, softmax_scale=0.07, stream=0)

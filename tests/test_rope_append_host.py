@@ -140,3 +140,32 @@ def test_binding_refuses_host_tensors(lib, fp8):
             with pytest.raises(libmla.MlaError, match="current CUDA device") as e:
                 fn(**a, stream=0)
             assert e.value.code == libmla.MLA_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_binding_refuses_types_of_the_same_size(lib, fp8):
+    """Each tensor in every other type of as many bytes an element."""
+    torch = pytest.importorskip("torch")
+    bf, i32 = torch.bfloat16, torch.int32
+    same = {1: [torch.int8, torch.float8_e5m2, torch.float8_e4m3fnuz], 2: [torch.float16, torch.int16],
+            4: [torch.int32, torch.float32]}
+    good = dict(kv_new=torch.zeros(2, 3, 576, dtype=bf),
+                kv_cache=torch.zeros(4, 64, 1, 576, dtype=torch.uint8 if fp8 else bf),
+                block_table=torch.zeros(2, 2, dtype=i32), cache_seqlens=torch.zeros(2, dtype=i32),
+                cos_sin=torch.zeros(64, 64), q_rope=torch.zeros(2, 3, 5, 64, dtype=bf),
+                q_out=torch.zeros(2, 3, 5, 64, dtype=bf), new_lens=torch.zeros(2, dtype=i32))
+    needs = dict(kv_new="kv_new must be bf16", kv_cache="kv_cache must be", cos_sin="cos_sin must be fp32",
+                 block_table="block_table must be int32", cache_seqlens="must be int32",
+                 new_lens="must be int32", q_rope="bf16", q_out="bf16")
+    if fp8:
+        good["scales"], needs["scales"] = torch.zeros(4, 4), "scales must be fp32"
+    fn = libmla.mla_rope_append_fp8 if fp8 else libmla.mla_rope_append
+    for k, why in needs.items():
+        for other in same[good[k].itemsize]:
+            if other == good[k].dtype:
+                continue
+            with pytest.raises(libmla.MlaError, match=why) as e:
+                fn(**{**good, k: good[k].view(other)}, stream=0)
+            assert e.value.code == libmla.MLA_ERR_INVALID_ARG
+    with pytest.raises(libmla.MlaError, match="current CUDA device"):
+        fn(**good, stream=0)
