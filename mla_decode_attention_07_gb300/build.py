@@ -2,8 +2,10 @@
 
 Each .cu under csrc/ is compiled to an object in parallel, then linked into
 ``_build/libmla.so`` next to this file; csrc/binding.c (the marshalling of some
-calls from Python, CPython C API) becomes ``_build/_binding.so``.  ``python -m
-mla_decode_attention_07_gb300.build [--verbose]``.
+calls from Python, CPython C API) becomes ``_build/_binding<suffix>``, with the
+running Python's own suffix for extension modules, so that another Python builds
+its own; without Python's headers it is left out, and those calls say so.
+``python -m mla_decode_attention_07_gb300.build [--verbose]``.
 """
 from __future__ import annotations
 
@@ -19,7 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libmla.so")
-BINDING = "_binding.so"
+BINDING = "_binding" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so")
 SOURCES = ["mla_api.cu", "mla_decode_sm103.cu", "mla_decode_narrow_sm103.cu", "mla_noalloc.cu",
            "gemm_sm103.cu", "attention_sm103.cu", "rope_append_sm103.cu",
            "mla_decode_fp8_sm103.cu"]
@@ -46,10 +48,18 @@ def _deps_mtime() -> float:
     return max(os.path.getmtime(p) for p in paths)
 
 
+def python_includes() -> list[str] | None:
+    """Where Python's headers are, or None."""
+    dirs = [sysconfig.get_paths()["include"], sysconfig.get_paths()["platinclude"]]
+    return dirs if any(os.path.exists(os.path.join(d, "Python.h")) for d in dirs) else None
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     binding = os.path.join(OUT_DIR, BINDING)
-    if (not force and os.path.exists(LIB) and os.path.exists(binding)
-            and min(os.path.getmtime(LIB), os.path.getmtime(binding)) >= _deps_mtime()):
+    headers = python_includes()
+    made = [LIB, binding] if headers else [LIB]
+    if (not force and all(os.path.exists(p) for p in made)
+            and min(os.path.getmtime(p) for p in made) >= _deps_mtime()):
         return LIB
     os.makedirs(OUT_DIR, exist_ok=True)
     cc = nvcc()
@@ -62,11 +72,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
         procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT,
                                             text=True)))
     tmp_binding = binding + f".tmp{os.getpid()}"
-    cmd = [os.environ.get("CC", "gcc"), "-O2", "-Wall", "-shared", "-fPIC", "-I", INCLUDE,
-           "-I", sysconfig.get_paths()["include"], "-I", sysconfig.get_paths()["platinclude"],
-           os.path.join(CSRC, "binding.c"), "-o", tmp_binding]
-    procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT,
-                                        text=True)))
+    if headers:
+        cmd = [os.environ.get("CC", "gcc"), "-O2", "-Wall", "-shared", "-fPIC", "-I", INCLUDE,
+               *(x for d in headers for x in ("-I", d)), os.path.join(CSRC, "binding.c"), "-o",
+               tmp_binding]
+        procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT,
+                                            text=True)))
+    else:
+        sys.stderr.write("Python's headers are missing: built without csrc/binding.c\n")
     failed = []
     for cmd, p in procs:
         out, _ = p.communicate()
@@ -78,7 +91,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
         raise RuntimeError("compiling failed:\n" + "\n".join(failed))
     tmp = LIB + f".tmp{os.getpid()}"
     subprocess.check_call([cc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs])
-    os.replace(tmp_binding, binding)
+    if headers:
+        os.replace(tmp_binding, binding)
     os.replace(tmp, LIB)
     return LIB
 

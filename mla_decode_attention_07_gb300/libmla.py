@@ -17,8 +17,11 @@ import os
 
 import numpy as np
 
+from .build import BINDING
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libmla.so")
+BINDING_PATH = os.path.join(_HERE, "_build", BINDING)
 
 MLA_OK = 0
 MLA_ERR_INVALID_ARG = -1
@@ -120,19 +123,25 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.mla_strerror.restype = ctypes.c_char_p
     if path is None:
         _lib = lib
-        _load_binding(p, lib)
     return lib
 
 
-def _load_binding(lib_path: str, lib: ctypes.CDLL) -> None:
-    """The compiled marshalling of the calls whose host time counts, beside the
-    library, with the addresses of the functions that it calls."""
+def _fast():
+    """The compiled marshalling of the calls whose host time counts, with the
+    addresses of the functions that it calls.  Loaded at the first of those
+    calls: the others do without it."""
     global _binding
-    path = os.path.join(os.path.dirname(lib_path), "_binding.so")
-    spec = importlib.util.spec_from_file_location("_binding", path)
-    mod = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(mod)
+    if _binding is not None:
+        return _binding
+    lib = load()
     import torch
+    try:
+        spec = importlib.util.spec_from_file_location("_binding", BINDING_PATH)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+    except (ImportError, OSError) as e:
+        raise RuntimeError(f"the compiled marshalling does not load ({BINDING_PATH}: {e}): run "
+                           "__graft_entry__.build() with this Python, whose headers it needs") from e
     mod.bind(*(ctypes.cast(fn, ctypes.c_void_p).value
                for fn in (lib.mla_rope_append, lib.mla_rope_append_fp8, lib.mla_decode_fp8,
                           lib.mla_decode_fp8_f32, lib.mla_decode_fp8_plan,
@@ -140,12 +149,7 @@ def _load_binding(lib_path: str, lib: ctypes.CDLL) -> None:
              torch._C._cuda_getCurrentRawStream, torch.bfloat16, torch.float32, torch.int32,
              torch.float8_e4m3fn, torch.uint8)
     _binding = mod
-
-
-def _fast():
-    if _binding is None:
-        load()
-    return _binding
+    return mod
 
 
 def _ptr(x) -> int | None:
