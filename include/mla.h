@@ -244,7 +244,9 @@ int mla_decode_sparse_f32(const void* q, const void* kv_cache, int num_pages,
  *   q        bf16 [batch, s_q, h_q, 576];  out bf16 [batch, s_q, h_q, 512]
  *   kv_cache e4m3 [num_pages, 64, 1, 576];  lse fp32 [batch, h_q, s_q]
  *   scales   fp32 [num_pages, 64 / scale_tokens], scale_tokens a power of two
- *            <= 64; finite, magnitude at most 2^60;  softmax_scale > 0
+ *            <= 64; finite, magnitude at most 2^60 (values under a scale below
+ *            2^-100, the least that the append stores, may count as zero);
+ *            softmax_scale > 0
  * all device; alignments as mla_decode, scales 4 bytes.  Codes and scales
  * past an entry's length are not used, whatever they hold.  A NaN among the
  * codes or scales an entry may see reaches every query row of that entry.

@@ -90,8 +90,15 @@ constexpr uint64_t kFDrainNs = 2000000ull;    // settle time after an abort
 constexpr float kFLn2 = 0.69314718055994530942f;
 constexpr float kTarget = 8.0f;   // log2 that the largest weight of a block of 32 tokens may have
 constexpr float kSlack = 40.0f;   // growth of the maximum over the reference that needs no rescale
-constexpr int kBlockMin = -120;   // smallest block exponent relative to the reference
-constexpr float kLogMin = 8.6736173798840355e-19f, kLogMax = 1.152921504606847e18f;  // 2^-60, 2^60
+constexpr int kBlockMin = -82;    // smallest block exponent relative to the reference
+// Scales whose logarithm is taken: 2^-100 (the least that the append stores) to
+// 2^60.  p = w / c is then up to 2^100 times w, and w up to 2^(8 + 40) over the
+// reference: O and the sums of p are both held times 2^-44 (O by V's scale factor
+// in the MMA), which keeps 2^20 such p, and one p at c = 2^60, finite and normal.
+constexpr float kLogMin = 7.8886090522101181e-31f, kLogMax = 1.152921504606847e18f;
+constexpr int kSumShift = 44;
+constexpr float kTotShift = 17592186044416.0f;   // 2^44
+static_assert(kBlockMin + 127 - kSumShift >= 1, "the sums' factor of a block stays normal");
 
 constexpr int kFStages = 5;
 constexpr uint32_t kFBox = 64 * 128;                       // 64 tokens x 128 dims, 128-byte swizzle
@@ -99,7 +106,7 @@ constexpr uint32_t kFRope = 4 * kFBox;                     // 64 tokens x 64 dim
 constexpr uint32_t kFStageBytes = kFRope + 64 * 64;        // one page: 36,864
 constexpr uint32_t kFTmemCols = 512;
 constexpr uint32_t kFColQ = 0;                             // [0, 144): Q, four codes a column
-constexpr uint32_t kFColSfa = 144;                         // scales of V (ones)
+constexpr uint32_t kFColSfa = 144;                         // scales of V (2^-44)
 constexpr uint32_t kFColSfb = 148;                         // 2 x 4 columns: scales of W
 constexpr uint32_t kFColS = 192;                           // one or two score tiles of 64 columns
 
@@ -591,10 +598,11 @@ __device__ __forceinline__ void f_softmax(const FCtx& x, const FWork& w, const F
     ++nq;
   };
 
-  // V's scales are one
+  // V's scales
   if (grp == 0) {
 #pragma unroll
-    for (uint32_t k = 0; k < 4; ++k) ptx::tmem_st1(x.tmem + lanes + kFColSfa + k, 0x7f7f7f7fu);
+    for (uint32_t k = 0; k < 4; ++k)
+      ptx::tmem_st1(x.tmem + lanes + kFColSfa + k, 0x01010101u * (uint32_t)(127 - kSumShift));
     ptx::tmem_wait_st();
     ptx::tc_fence_before();
   }
@@ -803,7 +811,7 @@ __device__ __forceinline__ void f_softmax(const FCtx& x, const FWork& w, const F
           one(std::integral_constant<int, 2>{});
           one(std::integral_constant<int, 3>{});
         }
-        const float bs = __uint_as_float(eb << 23);
+        const float bs = __uint_as_float((eb - (uint32_t)kSumShift) << 23);
         sum[h] = ptx::f2_fma(part, ptx::f2_pack(bs, bs), sum[h]);
       }
       ptx::fence_proxy_async_smem();
@@ -851,8 +859,12 @@ __device__ __forceinline__ void f_softmax(const FCtx& x, const FWork& w, const F
         if (slice == 0)
           ptx::st_shared_u32(x.sbase + S::kFac + (uint32_t)row * 4u,
                              __float_as_uint(tot == 0.f ? 0.f : 1.0f / tot));
-        else if (row < n_rows && slot_ok)
-          *lse_at[h] = tot == 0.f ? -INFINITY : (m[h] - kTarget + log2f(tot)) * kFLn2;
+        else if (row < n_rows && slot_ok) {
+          // unshifted where that stays finite: the logarithm has more bits there
+          const float l2 = tot < kTotShift ? log2f(tot * kTotShift)
+                                           : log2f(tot) + (float)kSumShift;   // NaN too
+          *lse_at[h] = tot == 0.f ? -INFINITY : (m[h] - kTarget + l2) * kFLn2;
+        }
       }
     }
     // every P.V of the entry is done once the last page's is

@@ -515,3 +515,50 @@ def test_decode_fp8_refuses_short_plans_and_host_tensors(torch_cuda):
     assert libmla.mla_check_device_error() == 0
     assert torch.all(out == 7) and torch.all(lse == 7)
     assert not np.isnan(run(torch, x, d=d)[0]).any()
+
+
+@pytest.mark.parametrize("h_q", [16, 32, 64])
+@pytest.mark.parametrize("exps", [(-70,), (-85,), (-100,), (-70, -85, -100)])
+@pytest.mark.parametrize("q_exp", [0, 1])
+def test_decode_fp8_all_scales_small(torch_cuda, h_q, exps, q_exp):
+    """Every scale of an entry far below one, down to the least that the append
+    stores: the weights keep their bits and out is the small average it is.  With
+    q_exp the query is as large as the scales are small, so that scores spread."""
+    x = Inputs(53, 2, h_q, [700, 90, 1], 1)
+    z = np.asarray(W.splitmix64(54, 0, x.scales.size) % np.uint64(len(exps))).reshape(x.scales.shape)
+    fresh = np.exp2(np.array(exps, dtype=np.float64))[z.astype(np.int64)].astype(np.float32)
+    x.scales = fresh * (1 + x.scales / x.scales.max()).astype(np.float32)
+    x.scales_gpu = np.where(np.isfinite(x.scales_gpu), x.scales, x.scales_gpu)
+    if q_exp:
+        x.q *= np.float32(2.0 ** (-max(exps) - 8))
+    d = to_gpu(torch_cuda, x)
+    out, lse, _ = run(torch_cuda, x, f32=True, d=d)
+    compare(x, out, lse)
+    ref = x.model()[0]
+    assert np.abs(out - ref).max() <= 0.25 * np.abs(ref).max()      # not near zero
+    assert_bf16_is_rounded_f32(run(torch_cuda, x, d=d)[0], out)
+
+
+@pytest.mark.parametrize("h_q", [16, 32, 64])
+@pytest.mark.parametrize("gain", [20.0, 60.0, 125.0])
+def test_decode_fp8_small_scales_that_weigh_most(torch_cuda, h_q, gain):
+    """Tokens of scale 1 with nothing in them first, then tokens of scale 2^-100
+    whose scores are up to `gain` higher in log2: their p is 2^100 times their
+    p c, far over the first tokens' reference."""
+    n = 64 * 20 + 9
+    x = Inputs(55, 1, h_q, [n], 1)
+    t = np.arange(n)
+    page, at = x.bt[0, t // 64], t % 64
+    x.codes[page, at, 0] &= 0x7F
+    first = (t // 64) % 4 < 2                                    # two pages of each kind in turn
+    x.codes[page[first], at[first], 0] = 0
+    x.scales[page, at] = np.where(first, 1.0, 2.0 ** -100)
+    x.q = np.abs(x.q)
+    k = M.E4M3[x.codes[page[~first], at[~first], 0]] * 2.0 ** -100
+    top = (x.q[0, 0].astype(np.float64) @ k.T).max() * SCALE * np.log2(np.e)
+    x.q = W.bf16_bits_to_float32(W.float32_to_bf16_bits((x.q.astype(np.float64) * (gain / top)).astype(np.float32)))
+    x.codes_gpu[page, at], x.scales_gpu[page, at] = x.codes[page, at], x.scales[page, at]
+    out, lse, _ = run(torch_cuda, x, f32=True)
+    compare(x, out, lse)
+    ref = x.model()[0]
+    assert np.abs(out - ref).max() <= 0.05 * ref.max()              # not near zero
