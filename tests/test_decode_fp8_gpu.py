@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 
 import fp8_model as M
+import plan_model
 from mla_decode_attention_07_gb300 import libmla
 from mla_decode_attention_07_gb300 import workloads as W
 from test_parity_gpu import assert_bf16_is_rounded_f32
@@ -562,3 +563,55 @@ def test_decode_fp8_small_scales_that_weigh_most(torch_cuda, h_q, gain):
     compare(x, out, lse)
     ref = x.model()[0]
     assert np.abs(out - ref).max() <= 0.05 * ref.max()              # not near zero
+
+
+@pytest.mark.parametrize("s_q, h_q", [(1, 5), (1, 32), (2, 16), (1, 64), (1, 128)])
+def test_decode_fp8_rescales_in_long_segments(torch_cuda, s_q, h_q):
+    """Workers that hold ten and more consecutive pages of an entry, rows whose
+    scores pass the running reference by more than 2^40 on every page, on every
+    second, once by 2^130, or never (flat, falling): the factors reach their own
+    rows' columns of O and sums.  The moves are counted on the host, from the
+    model's scores and the plan's page ranges."""
+    torch, B, L = torch_cuda, 170, 64 * 12 + 5
+    x = Inputs(56, s_q, h_q, [L], 1)
+    t = np.arange(L)
+    page, at = x.bt[0, t // 64], t % 64
+    c = 2.0 ** -6
+    x.scales[page, at] = c
+    x.codes[page, at, 0, 7] = M.e4m3_codes(16.0 * (t // 64))      # exact
+    x.codes[page, at, 0, 9] = M.e4m3_codes(np.where(t >= 64 * 6, 128.0, 0.0))
+    x.codes_gpu[page, at], x.scales_gpu[page, at] = x.codes[page, at], x.scales[page, at]
+    rng = np.random.default_rng(57)
+    q = rng.standard_normal((B, s_q, h_q, 576)) * 0.25
+    kind = (np.arange(h_q)[None, None] + np.arange(s_q)[None, :, None] + np.arange(B)[:, None, None]) % 5
+    per_page = np.choose(kind, [0.0, 50.0, -50.0, 30.0, 0.0])      # log2 units
+    q[..., 7] = per_page / (SCALE * np.log2(np.e) * c * 16)
+    q[..., 9] = np.where(kind == 4, 130.0, 0.0) / (SCALE * np.log2(np.e) * c * 128)
+    x.q = W.bf16_bits_to_float32(W.float32_to_bf16_bits(q.astype(np.float32)))
+    x.lens, x.bt = np.full(B, L, dtype=np.int32), np.repeat(x.bt, B, 0)
+    d = to_gpu(torch, x)
+    out, lse, _ = run(torch, x, f32=True, d=d)
+    compare(x, out, lse)
+    # what the kernel's reference does, from the page ranges
+    meta, _ = libmla.alloc_fp8_plan_and_workspace(B, s_q, h_q)
+    libmla.mla_decode_fp8_plan(d["lens"], s_q, h_q, meta)
+    plan = plan_model.decode(meta.cpu().numpy())
+    k = M.E4M3[x.codes[page, at, 0]] * c
+    longest, moves = 0, np.zeros((5, 13), dtype=int)
+    for w in range(plan["gused"]):
+        for b, pb, pe, _ in plan_model.segments(plan, w):
+            if pe - pb < 10:
+                continue
+            longest = max(longest, pe - pb)
+            z = (x.q[b].reshape(-1, 576).astype(np.float64) @ k.T) * SCALE * np.log2(np.e) + np.log2(c)
+            for i in range(s_q):
+                z[i * h_q:(i + 1) * h_q, L - s_q + 1 + i:] = -np.inf
+            ref = np.ceil(z[:, 64 * pb:64 * pb + 64].max(-1))
+            for pg in range(pb + 1, pe):
+                top = z[:, 64 * pg:64 * pg + 64].max(-1)
+                move = top > ref + 40
+                np.add.at(moves[:, pg], kind[b].reshape(-1)[move], 1)
+                ref = np.where(move, np.ceil(top), ref)
+    assert longest >= 10
+    assert (moves[1, 2:] > 0).all() and (moves[3, 2:] > 0).sum() >= 5 and moves[4, 6] > 0
+    assert not moves[0].any() and not moves[2].any()
