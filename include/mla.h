@@ -261,7 +261,8 @@ int mla_decode_sparse_f32(const void* q, const void* kv_cache, int num_pages,
  * need workspaces of their own.  A row with no visible key gets out = 0 and
  * lse = -inf; a page outside the pool is flagged as MLA_ERR_DEVICE_BOUNDS; a
  * tile_meta of another call is flagged as MLA_ERR_PLAN, nothing behind its end
- * is read, and out and lse stay as they were.
+ * is read, and out and lse stay as they were.  out and lse do not depend on
+ * max_pages, in no bit.
  * Defined by: as mla_decode, over the 8-bit form of its cache.
  * Errors: as mla_decode. */
 int mla_decode_fp8(const void* q, const void* kv_cache, const float* scales, int scale_tokens,

@@ -1096,6 +1096,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
 // Entries without pages get out = 0, lse = -inf.
 constexpr int kF8CombineCtas = 7;   // an SM
 constexpr int kF8ShareParts = 8;    // with so many the warps share the splits
+constexpr int kF8WidePages = 15;
 constexpr int kF8MaxSplits = 256;   // an entry has at most as many splits as a tile's CTAs
 
 template <int parts, int kWarps>
@@ -1333,14 +1334,19 @@ cudaError_t launch_decode_fp8(const CUtensorMap& kv_lat, const CUtensorMap& kv_r
   // share the splits and an entry may have 16 or more (from the workers and the
   // pages of the block table), 16 warps: one entry of 20000 tokens with 64 heads
   // 32.9 -> 21.0 us, of 4096 with 16 heads 14.2 -> 13.3; with fewer splits they
-  // only start later (four entries of up to 300 tokens, 32 heads 13.4 -> 14.4).
+  // only start later (four entries of up to 300 tokens, 32 heads 13.4 -> 14.4,
+  // which a table as wide as a context limit costs such a batch).
+  // The table's width reaches no bit of the results: an entry that it bounds to
+  // fewer than kF8WidePages least shares has at most 16 splits (P pages touch at
+  // most (P - 1 + m - 1) / m + 1 workers of m units or more), and those both forms
+  // add up in the same order, four a warp.
   const int64_t quads = (int64_t)p.batch * tiles * (rows_t / 4);
   const int64_t cap = kF8CombineCtas * (int64_t)num_sms;
   const int parts = quads * kF8ShareParts <= cap ? kF8ShareParts : quads * 2 <= cap ? 2 : 1;
   const int64_t jobs = quads * parts;
-  const int by_workers = p.workers / tiles / p.batch, by_pages = p.max_pages / f8_min_units(rows_t);
   const bool wide = parts == kF8ShareParts && jobs <= 2 * (int64_t)num_sms &&
-                    (by_workers < by_pages ? by_workers : by_pages) >= 16;
+                    p.workers / tiles / p.batch >= 16 &&
+                    p.max_pages / f8_min_units(rows_t) >= kF8WidePages;
   cfg.gridDim = dim3((unsigned)(jobs < cap ? jobs : cap));
   cfg.blockDim = dim3(wide ? 512 : 128);
   cfg.dynamicSmemBytes = 0;

@@ -615,3 +615,23 @@ def test_decode_fp8_rescales_in_long_segments(torch_cuda, s_q, h_q):
     assert longest >= 10
     assert (moves[1, 2:] > 0).all() and (moves[3, 2:] > 0).sum() >= 5 and moves[4, 6] > 0
     assert not moves[0].any() and not moves[2].any()
+
+
+@pytest.mark.parametrize("h, pages", [
+    (16, [38, 45, 47, 16, 47, 47, 27]),          # 17 splits of an entry
+    (16, [17, 44, 44, 44, 44]), (5, [44]), (16, [4, 5]), (16, [50, 50, 50]), (16, [1]),
+    (32, [30, 30, 30]), (32, [5, 5, 5, 5]), (32, [4, 32, 5, 32, 17]), (20, [28, 28]),
+    (64, [28, 27, 28, 9]), (64, [300]), (128, [30, 30, 30]), (128, [29, 60]), (16, [20] * 30)])
+def test_decode_fp8_table_width_changes_no_bit(torch_cuda, h, pages):
+    """A block table just as wide as its longest entry, and one as wide as a
+    context limit."""
+    torch = torch_cuda
+    lens = [64 * p - 7 * (i % 3) for i, p in enumerate(pages)]
+    x = Inputs(58, 1, h, lens, 1)
+    d = to_gpu(torch, x)
+    tight = run(torch, x, f32=True, d=d)
+    for width in (len(x.bt[0]) + 1, 2 * len(x.bt[0]), 2048):
+        bt = torch.full((len(lens), width), x.pages, dtype=torch.int32, device="cuda")
+        bt[:, :d["bt"].shape[1]] = d["bt"]
+        out, lse, _ = run(torch, x, f32=True, d=dict(d, bt=bt))
+        assert np.array_equal(out, tight[0]) and np.array_equal(lse, tight[1]), width
