@@ -337,7 +337,8 @@ int mla_cache_append(const void* kv_new, void* kv_cache, int num_pages,
  *   kv_cache  bf16 [num_pages, 64, 1, 576];  block_table int32 [batch, max_pages]
  *   cache_seqlens, new_lens int32 [batch];   cos_sin fp32 [max_positions, 64]
  * all device; strides in elements, multiples of 8; kv_new, q_rope, q_out,
- * kv_cache and cos_sin 16-byte aligned.  Rows i >= n_b are not written, and
+ * kv_cache and cos_sin 16-byte aligned.  Rows of q_out may not lie on one
+ * another (MLA_ERR_INVALID_ARG).  Rows i >= n_b are not written, and
  * what they hold does not matter.  Inputs and outputs do not overlap
  * otherwise.  A position below 0, past the block table or past the table of
  * angles, a page outside the pool and a new_lens[b] outside [0, s_new] are

@@ -28,6 +28,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "mla.h"
 #include "mla_internal.h"
 
@@ -381,6 +383,23 @@ __global__ void __launch_bounds__(kRopeThreads) mla_rope_append_fp8_kernel(const
 
 bool al(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+// Whether rows of kRopeDims at these three sizes and strides lie apart: taken by
+// rising stride, each dim steps over all that the ones before it cover (any
+// order of the dims, any slice).
+bool apart(int n0, int64_t st0, int n1, int64_t st1, int n2, int64_t st2) {
+  struct {
+    int64_t n, step;
+  } d[3] = {{n0, st0}, {n1, st1}, {n2, st2}};
+  std::sort(d, d + 3, [](auto& x, auto& y) { return x.step < y.step; });
+  int64_t cover = kRopeDims;
+  for (auto& k : d) {
+    if (k.n == 1) continue;
+    if (k.step < cover || k.step > (INT64_MAX - cover) / (k.n - 1)) return false;
+    cover += (k.n - 1) * k.step;
+  }
+  return true;
+}
+
 // Checks shared by the two entry points; fills everything but the pages.
 int prepare_rope(RopeArgs* a, const void* kv_new, int64_t kv_sb, int64_t kv_ss, const void* q_rope,
                  int64_t q_sb, int64_t q_ss, int64_t q_sh, void* q_out, int64_t qo_sb,
@@ -401,9 +420,7 @@ int prepare_rope(RopeArgs* a, const void* kv_new, int64_t kv_sb, int64_t kv_ss, 
         ((q_sb | q_ss | q_sh | qo_sb | qo_ss | qo_sh) & 7) || q_sb < 0 || q_ss < 0 || q_sh < 0)
       return MLA_ERR_INVALID_ARG;
     // rows that are written must not lie on one another
-    if ((h_q > 1 && qo_sh < kRopeDims) || (s_new > 1 && qo_ss < kRopeDims) ||
-        (batch > 1 && qo_sb < kRopeDims))
-      return MLA_ERR_INVALID_ARG;
+    if (!apart(batch, qo_sb, s_new, qo_ss, h_q, qo_sh)) return MLA_ERR_INVALID_ARG;
   }
   a->kv_new = static_cast<const __nv_bfloat16*>(kv_new);
   a->kv_sb = kv_sb;

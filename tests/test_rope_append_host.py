@@ -169,3 +169,26 @@ def test_binding_refuses_types_of_the_same_size(lib, fp8):
             assert e.value.code == libmla.MLA_ERR_INVALID_ARG
     with pytest.raises(libmla.MlaError, match="current CUDA device"):
         fn(**good, stream=0)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("kw", [
+    dict(s_new=2, os=64, oh=64), dict(s_new=3, os=512, oh=64, h=16), dict(batch=2, ob=64, oh=64),
+    dict(batch=2, s_new=2, ob=1024, os=1024), dict(batch=3, s_new=2, h=1, ob=64, os=128),
+    dict(batch=2, s_new=1, h=2, ob=96, oh=64)], ids=str)
+def test_rope_append_rejects_query_rows_on_one_another(lib, fp8, kw):
+    """Strides of q_out that put two rows on the same elements."""
+    assert _call(lib, fp8, **kw) == libmla.MLA_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("kw", [
+    dict(s_new=2, os=1024, oh=64), dict(batch=2, s_new=3, ob=64 * 6 * 16, os=64, oh=64 * 6, qs=64),
+    dict(batch=2, s_new=2, os=128 * 16, ob=64, oh=128),          # entries inside the heads
+    dict(batch=1, s_new=2, ob=0, os=576 * 16, oh=576), dict(batch=4, s_new=1, os=0, ob=1024, oh=64),
+    dict(batch=2, s_new=1, h=1, ob=64, oh=0, os=0)], ids=str)
+def test_rope_append_takes_query_rows_in_any_order(lib, fp8, kw):
+    from conftest import gpu_available
+    if gpu_available():
+        pytest.skip("the addresses are made up")
+    assert _call(lib, fp8, **kw) in (libmla.MLA_ERR_CUDA, libmla.MLA_ERR_UNSUPPORTED_DEVICE)
