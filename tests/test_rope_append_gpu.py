@@ -330,3 +330,43 @@ def test_append_pages_past_4_gb(torch_cuda, fp8):
         if far:
             assert not cache[:pool - c.pages].view(torch.int32).any()
     assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: f"s{c[0]}_h{c[4]}_g{c[7]}")
+def test_append_fp8_bits_of_scales_and_latents(torch_cuda, case):
+    """Where the largest magnitude of a block lies in its latent dims (bf16, not
+    turned), the scale, every latent code and every code that is stored anew are
+    determined: quotients rounded to fp32, then codes to the nearest, halves to
+    even."""
+    torch, c = torch_cuda, Case(*case, rope_scale=0.125)
+    g, f32 = to_gpu(torch, c), np.float32
+    libmla.mla_rope_append_fp8(g["kv"], g["codes"], g["scales"], g["bt"], g["lens"], g["cs"],
+                               g["q"], g["q_out"], new_lens=g["new"], interleaved=c.il)
+    assert libmla.mla_check_device_error() == 0
+    codes, scales = g["codes"].cpu().numpy().reshape(-1, 576), g["scales"].cpu().numpy().reshape(-1)
+    blocks = {}
+    for b, i, t, row, val, *_ in c.rows():
+        blocks.setdefault((b, row // c.G), []).append((t, row, val))
+    checked = grown = 0
+    for (b, blk), toks in blocks.items():
+        if max(np.abs(v[512:]).max() for _, _, v in toks) > max(np.abs(v[:512]).max() for _, _, v in toks) / 2:
+            continue
+        amax = max(np.abs(v[:512]).max() for _, _, v in toks)
+        fresh = max(f32(amax / 448), f32(M.SCALE_MIN))
+        start, t0 = int(c.lens[b] - c.new_lens[b]), toks[0][0] - toks[0][1] % c.G
+        old = c.scales.reshape(-1)[blk] if t0 < start else f32(0)
+        scale = max(fresh, old)
+        assert scales[blk] == scale
+        for _, row, v in toks:
+            quotient = v[:512] * 448 / amax if scale == fresh else v[:512] / np.float64(scale)
+            assert np.array_equal(codes[row, :512], M.e4m3_codes(quotient.astype(f32))), row
+        before = c.codes.reshape(-1, 576)[blk * c.G:blk * c.G + max(start - t0, 0)]
+        if scale > old:
+            ratio = f32(np.float64(old) / np.float64(scale))
+            before = M.e4m3_codes(M.E4M3[before].astype(f32) * ratio)
+            grown += len(before) > 0
+        assert np.array_equal(codes[blk * c.G:blk * c.G + len(before)], before)
+        checked += 1
+    assert checked > 0
+    if c.G == 16:
+        assert grown > 0
