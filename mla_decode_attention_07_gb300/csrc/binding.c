@@ -3,10 +3,10 @@
  * library could not see (types, shapes, strided tables, short plans, tensors on
  * the host or another device), and calls the C ABI.
  * Plain CPython C API; the functions' addresses come from libmla.py, which has
- * loaded the library.  An 8-bit append takes 5.3 us of a Grace host, its launch
- * 2.1 among them, against 9.3 with the same checks in Python and the call
- * through ctypes (whose conversions alone take 2.2); with a small batch that is
- * the call's time (1 token, 16 heads: 10.9 -> 6.2 us). */
+ * loaded the library.  An 8-bit append takes 5.5 us of a Grace host, its launch
+ * 2.1 among them, against 9.3 with fewer checks in Python and the call through
+ * ctypes (whose conversions alone take 2.2); with a small batch that is the
+ * call's time (1 token, 16 heads: 10.9 -> 5.9 us). */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 #include <stdint.h>

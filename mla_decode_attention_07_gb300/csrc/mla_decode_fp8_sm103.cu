@@ -19,7 +19,8 @@
 //    as its scale factor (block-scaled MMA), taken against a whole-numbered
 //    reference of the row, in log2 units of p c.  It has 8 bits, so the
 //    reference is set at an entry's first page and moves only when a later
-//    score passes it by 2^40: O and the sums are hardly ever rescaled.
+//    score passes it by 2^40: O and the sums are hardly ever rescaled.  Both
+//    are held times 2^-44, so that the p of a token whose c is 2^-100 fits.
 // The sums of p_t, the maxima, scores and O are fp32.
 //
 // Layout of the work.  One CTA, 64 query rows, whole pages:
@@ -52,14 +53,16 @@
 // 576 (S) + 608 cycles, the shared memory 1100 to feed them (144 KB a page),
 // the softmax warps about 1700: reading S to its maxima 650, barrier 120 to
 // 190, weights 600, fences and waits 270; the next page's S is there before
-// they ask for it.  132 x 2 x 128 heads over 8192 tokens take 430 us: 1.4
-// PFLOP/s of 2 x 1088 a row and key, and the split doubles what the MMAs do.
+// they ask for it.  132 x 2 x 128 heads over 8192 tokens take 430 to 467 us
+// without their plan, as the card's power limit lets: 1.3 to 1.4 PFLOP/s of 2 x
+// 1088 a row and key, and the split doubles what the MMAs do.
 // Tried and not kept there (us for that call; the kernel at the time in
 // brackets): two score tiles, with the query's last 128 dims in shared memory
 // for them, 456 (435); block exponents guessed from the pages before and the
 // maxima checked after the weights 463 (440, a guess of 128 fails too often);
-// all of a query's loads at once 513 (477).  With 16 rows the cache's bytes
-// bound it: 8 x 16 heads over 65536 tokens 51 us, 5.9 TB/s.
+// all of a query's loads at once 513 (477).  With up to 32 rows the cache's
+// bytes bound it: over 65536 tokens 8 x 16 heads take 53 us (5.7 TB/s), 8 x 32
+// heads 57 (5.4 TB/s), without plan and combine.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -1,10 +1,10 @@
 """ctypes binding of libmla (the C ABI in include/mla.h).
 
-Argument marshalling only (that of the rotating appends and of the 8-bit
-decode is compiled, csrc/binding.c): every step of the decode runs in the
-library's CUDA kernels.  Device buffers are torch tensors (their data pointers are
-passed through); torch is used for memory and streams, nothing else.  The
-library must have been built (``__graft_entry__.build()`` or
+Argument marshalling only: every step of the decode runs in the library's CUDA
+kernels.  (That of the rotating appends and of the 8-bit decode is compiled,
+csrc/binding.c, and loaded when first needed.)  Device buffers are torch tensors
+(their data pointers are passed through); torch is used for memory and streams,
+nothing else.  The library must have been built (``__graft_entry__.build()`` or
 ``python -m mla_decode_attention_07_gb300.build``); loading fails loudly
 otherwise, and on a device that is not sm_103 the calls return
 MLA_ERR_UNSUPPORTED_DEVICE.
