@@ -1099,7 +1099,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
 // Entries without pages get out = 0, lse = -inf.
 constexpr int kF8CombineCtas = 7;   // an SM
 constexpr int kF8ShareParts = 8;    // with so many the warps share the splits
-constexpr int kF8WidePages = 15;
+constexpr int kF8WidePages = 15;    // least shares a table holds from which they may be 16
 constexpr int kF8MaxSplits = 256;   // an entry has at most as many splits as a tile's CTAs
 
 template <int parts, int kWarps>
